@@ -190,12 +190,18 @@ muon_status muon_ns_orthogonalize(muon_ctx* ctx, const void* const* X, void* con
                                   int batch, int rows, int cols, int dtype, float eps,
                                   void* stream);
 
-/* Device-side status of the most recent call on this context.  Synchronises
- * the stream of that call, then copies up to `capacity` per-matrix flag words
- * (MUON_FLAG_*) into `flags` (may be NULL) and the number of matrices into
- * *count (may be NULL; 0 after a muon_expert_* call).  Returns MUON_ERR_TIMEOUT
- * if any kernel wait ran out, else MUON_ERR_INVALID_ARG if expert offsets were
- * bad, else MUON_ERR_NONFINITE if any matrix was flagged, else MUON_OK. */
+/* Device-side status of the most recent call on this context, and of every
+ * expert and block call since this was last asked: those add up until they
+ * are reported here, once, whatever else the context did in between (steps of
+ * whole matrices, other block calls, replays of captured graphs).  Synchronises
+ * the stream of the most recent call (synchronise other streams, and those
+ * that graphs are replayed on, first), then copies up to `capacity` per-matrix
+ * or per-block flag words (MUON_FLAG_*) of that call into `flags` (may be NULL)
+ * and their number into *count (may be NULL; 0 after a muon_expert_* call).
+ * Returns MUON_ERR_TIMEOUT if any kernel wait ran out, else
+ * MUON_ERR_INVALID_ARG if expert offsets were bad, else MUON_ERR_NONFINITE if
+ * any matrix of the call, or any block since the last report, was flagged,
+ * else MUON_OK. */
 muon_status muon_get_status(muon_ctx* ctx, int* flags, int capacity, int* count);
 
 /* ||U||_F per matrix of the most recent call (same order as the flags). */
@@ -302,8 +308,7 @@ muon_status muon_adamw_step(void* const* W, const void* const* G, float* const* 
  * are multiplied with fp32 accumulation and rounded once; fp32 ones are split into three bf16 planes whose
  * six leading products are accumulated in fp32 (fp32 infinities and values above 3.38e38 become NaN).
  * Offsets and sizes: 0 <= tokens <= 2^30, 1 <= rows, cols <= 32768, 1 <= experts <= MUON_MAX_EXPERTS.
- * Device-side status (a wait that ran out, bad offsets) is collected over the muon_expert_* and
- * block calls of a context until muon_get_status is called or another step begins. */
+ * Device-side status (a wait that ran out, bad offsets) is kept until muon_get_status reports it. */
 typedef struct {
   const int* offsets; /* DEVICE, experts + 1 ints                          */
   int experts;        /* weights in the stack                              */

@@ -525,21 +525,27 @@ class Muon:
 
     # -------------------------------------------------------------- status
     def status(self):
-        """(status code, per-matrix or per-block flags) of the last call; synchronises its stream."""
-        cnt = ctypes.c_int()
-        self.lib.muon_get_status(self.handle, None, 0, ctypes.byref(cnt))
-        cap = max(cnt.value, 1)
-        flags = (ctypes.c_int * cap)()
+        """(status code, per-matrix or per-block flags) of the last call; synchronises its stream.
+
+        The code also covers every expert and block call since the last report: 5 (a matrix or block was
+        not finite) and 6 (a wait ran out) are returned, bad expert offsets raise.  Each is reported once.
+        """
+        cap = max(self._results(), 1)
+        flags, cnt = (ctypes.c_int * cap)(), ctypes.c_int()
         st = self.lib.muon_get_status(self.handle, flags, cap, ctypes.byref(cnt))
         if st not in (MUON_OK, 5, 6):
             self._check(st, "muon_get_status")
         return st, list(flags[:cnt.value])
 
-    def norms(self):
+    def _results(self):
+        """How many matrices or blocks the last call has results of (leaves the status as it is)."""
         cnt = ctypes.c_int()
-        self.lib.muon_get_status(self.handle, None, 0, ctypes.byref(cnt))
-        cap = max(cnt.value, 1)
-        nu = (ctypes.c_float * cap)()
+        self._check(self.lib.muon_get_norms(self.handle, (ctypes.c_float * 1)(), 0, ctypes.byref(cnt)), "muon_get_norms")
+        return cnt.value
+
+    def norms(self):
+        cap = max(self._results(), 1)
+        nu, cnt = (ctypes.c_float * cap)(), ctypes.c_int()
         self._check(self.lib.muon_get_norms(self.handle, nu, cap, ctypes.byref(cnt)), "muon_get_norms")
         return list(nu[:cnt.value])
 

@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) block_kernel(const __grid_cons
   if (tid == 0 && rank == 0) {
     P.nu[b] = nu;
     P.flags[b] = fine ? 0 : MUON_FLAG_NONFINITE;
+    if (!fine) atomicOr(P.status, kStatusNonfinite);
   }
 
   if (fine) {  // the same in every CTA of the cluster

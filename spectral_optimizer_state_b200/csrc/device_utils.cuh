@@ -16,6 +16,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // Device status word bits.
 constexpr int kStatusTimeout = 1;
 constexpr int kStatusBadSegments = 2;  // expert offsets outside the rows, or decreasing
+constexpr int kStatusNonfinite = 4;    // a block was flagged (block calls; whole matrices have flags alone)
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

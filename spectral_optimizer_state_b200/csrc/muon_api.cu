@@ -156,6 +156,8 @@ struct muon_ctx {
   int* d_flags = nullptr;
   unsigned* d_counters = nullptr;
   float* d_partials = nullptr;
+  // [0]: the last whole-matrix call's, cleared as one begins; [1]: what expert and block calls have reported
+  // since muon_get_status last took it; [2]: what it took
   int* d_status = nullptr;
   unsigned* d_done = nullptr;  // [kMaxProblems][MUON_MAX_BATCH] phase-completion counters
   // MUON_OVERLAP=1: momentum passes of later groups and applies of earlier groups run on a side
@@ -174,7 +176,6 @@ struct muon_ctx {
   int last_count = 0;
   cudaStream_t last_stream = nullptr;
   bool pending = false;
-  bool status_read = false;     // muon_get_status has seen an error word that the next expert / block call clears
   bool captured = false;        // a call was captured into a CUDA graph: the buffers never move again
   // device staging for gradients that arrive from host memory
   void* d_stage = nullptr;
@@ -742,12 +743,40 @@ muon_status run(muon_ctx* c, std::vector<GroupPlan>& plans, const muon_hparams* 
   return MUON_OK;
 }
 
-// The expert and block calls clear the status word only after an error was read (a memset per call
-// would cost as much as their smallest kernels); errors of several calls collect until then.
-muon_status begin_collected(muon_ctx* c, cudaStream_t s) {
-  if (!c->status_read) return MUON_OK;
-  MUON_CUDA(cudaMemsetAsync(c->d_status, 0, sizeof(int), s), "clear status");
-  c->status_read = false;
+// Expert and block calls add to a status word of their own, which nothing but muon_get_status clears (a
+// memset a call would cost as much as their smallest kernels, and captured it would wipe what earlier
+// replays reported).
+int* collected_status(const muon_ctx* c) { return c->d_status + 1; }
+
+__global__ void take_status_kernel(int* word, int* taken) { *taken = atomicExch(word, 0); }
+
+// The last call's status and flags and, with `take`, what expert and block calls have reported since this was
+// last asked.
+muon_status last_status(muon_ctx* c, int* flags, int capacity, int* count, bool take) {
+  DeviceGuard guard(c->device);
+  if (count) *count = c->last_count;
+  if (!c->pending) return MUON_OK;
+  MUON_CUDA(cudaStreamSynchronize(c->last_stream), "stream synchronize");
+  int word[2] = {0, 0};
+  MUON_CUDA(cudaMemcpy(word, c->d_status, sizeof(word), cudaMemcpyDeviceToHost), "read status");
+  if (!take) word[1] = 0;
+  if (word[1] != 0) {  // taken in one exchange: what another stream adds meanwhile is kept for the next report
+    take_status_kernel<<<1, 1, 0, c->last_stream>>>(collected_status(c), c->d_status + 2);
+    MUON_CUDA(cudaGetLastError(), "take status");
+    MUON_CUDA(cudaMemcpyAsync(&word[1], c->d_status + 2, sizeof(int), cudaMemcpyDeviceToHost, c->last_stream), "read status");
+    MUON_CUDA(cudaStreamSynchronize(c->last_stream), "stream synchronize");
+  }
+  const int status = word[0] | word[1];
+  std::vector<int> f(c->last_count);
+  if (c->last_count > 0)
+    MUON_CUDA(cudaMemcpy(f.data(), c->out_flags, sizeof(int) * c->last_count, cudaMemcpyDeviceToHost),
+              "read flags");
+  if (flags) std::memcpy(flags, f.data(), sizeof(int) * std::min(capacity, c->last_count));
+  if (status & kStatusTimeout) return MUON_ERR_TIMEOUT;
+  if (status & kStatusBadSegments) return MUON_ERR_INVALID_ARG;
+  if (status & kStatusNonfinite) return MUON_ERR_NONFINITE;
+  for (int v : f)
+    if (v & MUON_FLAG_NONFINITE) return MUON_ERR_NONFINITE;
   return MUON_OK;
 }
 
@@ -870,8 +899,6 @@ muon_status run_experts(muon_ctx* c, const muon_experts* ex, ExpertMode mode, Op
   const size_t need = (pa ? operand_bytes(qa) : 0) + (pb ? operand_bytes(qb) : 0);
   muon_status st = ensure_aux(c, need, s);
   if (st != MUON_OK) return st;
-  st = begin_collected(c, s);
-  if (st != MUON_OK) return st;
   char* at = static_cast<char*>(c->d_aux);
   PackParams packs;
   packs.count = 0;
@@ -918,7 +945,7 @@ muon_status run_experts(muon_ctx* c, const muon_experts* ex, ExpertMode mode, Op
   p.tokens = ex->tokens;
   p.in_f32 = f32;
   p.split = split;
-  p.status = c->d_status;
+  p.status = collected_status(c);
   const bool pair = !split && expert_pair(mode, f32, p.features, p.rows, ex->tokens, ex->experts);
   const int fm = pair ? 256 : 128;
   const long long nf = (p.features + fm - 1) / fm;
@@ -1061,7 +1088,7 @@ muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* h
   p.scale_mode = step ? hp->scale_mode : MUON_SCALE_NONE;
   p.k = c->k;
   std::memcpy(p.abc, c->coeffs, sizeof(float) * 3 * c->k);
-  p.status = c->d_status;
+  p.status = collected_status(c);
   if (total > c->cap_blocks) {
     const muon_status st = may_grow(c, s, "the per-block results");
     if (st != MUON_OK) return st;
@@ -1079,8 +1106,6 @@ muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* h
     c->cap_blocks = static_cast<int>(total);
   }
   note_capture(c, s);
-  const muon_status st = begin_collected(c, s);
-  if (st != MUON_OK) return st;
   p.nu = c->d_nu_blocks;
   p.flags = c->d_flags_blocks;
   MUON_CUDA(launch_blocks(p, static_cast<int>(total), tall, f32, smem, s), "block step");
@@ -1172,12 +1197,12 @@ muon_status muon_create(muon_ctx** out, int device) {
       c->side = nullptr;  // everything runs on the caller's stream
     }
   }
-  if (cudaMalloc(&c->d_status, sizeof(int)) != cudaSuccess) {
+  if (cudaMalloc(&c->d_status, 3 * sizeof(int)) != cudaSuccess) {
     note_alloc_failure();
     delete c;
     return MUON_ERR_ALLOC;
   }
-  cudaMemset(c->d_status, 0, sizeof(int));
+  cudaMemset(c->d_status, 0, 3 * sizeof(int));
   if (cudaMalloc(&c->d_done, sizeof(unsigned) * kMaxProblems * MUON_MAX_BATCH) != cudaSuccess) {
     note_alloc_failure();
     cudaFree(c->d_status);
@@ -1283,30 +1308,14 @@ muon_status muon_ns_orthogonalize(muon_ctx* c, const void* const* X, void* const
 
 muon_status muon_get_status(muon_ctx* c, int* flags, int capacity, int* count) {
   if (!c || capacity < 0) return MUON_ERR_INVALID_ARG;
-  DeviceGuard guard(c->device);
-  if (count) *count = c->last_count;
-  if (!c->pending) return MUON_OK;
-  MUON_CUDA(cudaStreamSynchronize(c->last_stream), "stream synchronize");
-  int status = 0;
-  MUON_CUDA(cudaMemcpy(&status, c->d_status, sizeof(int), cudaMemcpyDeviceToHost), "read status");
-  std::vector<int> f(c->last_count);
-  if (c->last_count > 0)
-    MUON_CUDA(cudaMemcpy(f.data(), c->out_flags, sizeof(int) * c->last_count, cudaMemcpyDeviceToHost),
-              "read flags");
-  if (flags) std::memcpy(flags, f.data(), sizeof(int) * std::min(capacity, c->last_count));
-  c->status_read = status != 0;
-  if (status & kStatusTimeout) return MUON_ERR_TIMEOUT;
-  if (status & kStatusBadSegments) return MUON_ERR_INVALID_ARG;
-  for (int v : f)
-    if (v & MUON_FLAG_NONFINITE) return MUON_ERR_NONFINITE;
-  return MUON_OK;
+  return last_status(c, flags, capacity, count, true);
 }
 
 muon_status muon_get_norms(muon_ctx* c, float* nu, int capacity, int* count) {
   if (!c || !nu || capacity < 0) return MUON_ERR_INVALID_ARG;
   DeviceGuard guard(c->device);
   if (count) *count = c->last_count;
-  if (!c->pending || c->last_count == 0) return MUON_OK;
+  if (!c->pending || c->last_count == 0 || capacity == 0) return MUON_OK;
   MUON_CUDA(cudaStreamSynchronize(c->last_stream), "stream synchronize");
   MUON_CUDA(cudaMemcpy(nu, c->out_nu, sizeof(float) * std::min(capacity, c->last_count),
                        cudaMemcpyDeviceToHost),
@@ -1449,7 +1458,7 @@ muon_status muon_step_groups_host(muon_ctx* c, const muon_group* groups, int ngr
     MUON_CUDA(cudaMemcpyAsync(flags_host, c->out_flags, sizeof(int) * c->last_count, cudaMemcpyDeviceToHost, s),
               "flag download");
   MUON_CUDA(cudaStreamSynchronize(s), "stream synchronize");
-  return muon_get_status(c, nullptr, 0, nullptr);
+  return last_status(c, nullptr, 0, nullptr, false);  // this call's: others' stay for muon_get_status
 }
 
 muon_status muon_power_iteration(muon_ctx* c, const void* const* W, float* const* u, float* const* v,
@@ -1677,7 +1686,10 @@ muon_status muon_expert_matmul(muon_ctx* c, const muon_experts* ex, const void* 
   if (!rows_ok(X, ldx, ex->tokens, in) || !rows_ok(Y, ldy, ex->tokens, out) ||
       !stack_ok(W, ldw, sw, ex->experts, ex->rows, ex->cols, false))
     return MUON_ERR_INVALID_ARG;
-  if (ex->tokens == 0) return MUON_OK;
+  if (ex->tokens == 0) {
+    c->last_count = 0;
+    return MUON_OK;
+  }
   if (Y == X || Y == W) return MUON_ERR_INVALID_ARG;
   DeviceGuard guard(c->device);
   ExpertParams p;
