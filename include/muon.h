@@ -299,8 +299,9 @@ muon_status muon_adamw_step(void* const* W, const void* const* G, float* const* 
  * Token rows are sorted by expert: rows offsets[e] .. offsets[e+1]-1 belong to expert e, offsets
  * being a DEVICE array of experts + 1 ints that the kernels read (no host synchronisation).  An
  * expert may have no row; rows before offsets[0] and from offsets[experts] on belong to none.
- * Offsets that decrease or leave 0 .. tokens make the call compute nothing; muon_get_status then
- * returns MUON_ERR_INVALID_ARG.
+ * Offsets that decrease or leave 0 .. tokens make the call compute nothing: outputs stay as they
+ * were, but those that hold nothing yet (clear_rest, muon_expert_grad_new) become zero.
+ * muon_get_status then returns MUON_ERR_INVALID_ARG.
  * Matrices are row-major with a row stride (ld*) and, for the stacks, an expert stride (s*), in
  * elements; the last dimension is contiguous.  Any sizes, strides and element alignments are taken:
  * bf16 operands whose rows do not start on 16-byte boundaries, and fp32 operands of calls with more than
@@ -332,6 +333,12 @@ muon_status muon_expert_matmul(muon_ctx* ctx, const muon_experts* ex, const void
 muon_status muon_expert_grad(muon_ctx* ctx, const muon_experts* ex, const void* dY, long long ldy,
                              const void* X, long long ldx, void* G, long long ldg, long long sg,
                              int out_dtype, float beta, float scale, void* stream);
+
+/* The same with beta == 0 for a G that holds nothing yet: every element of it is written, zeros if the
+ * offsets are bad. */
+muon_status muon_expert_grad_new(muon_ctx* ctx, const muon_experts* ex, const void* dY, long long ldy,
+                                 const void* X, long long ldx, void* G, long long ldg, long long sg,
+                                 int out_dtype, float scale, void* stream);
 
 /* Muon on blocks: every matrix is cut into blocks of block_rows x block_cols (the last block row and
  * column may be smaller) and each block is stepped, or orthogonalised, on its own -- heads of an input

@@ -39,7 +39,7 @@ EXPORTS = (
     "muon_ns_orthogonalize", "muon_get_status", "muon_get_norms", "muon_workspace_bytes",
     "muon_profile_enable", "muon_profile_read", "muon_momentum_norm_noalloc", "muon_adamw_step",
     "muon_power_iteration", "muon_min_singular", "muon_step_capped", "muon_expert_matmul", "muon_expert_grad",
-    "muon_step_blocks", "muon_ns_orthogonalize_blocks",
+    "muon_expert_grad_new", "muon_step_blocks", "muon_ns_orthogonalize_blocks",
 )
 KERNEL_KINDS = ("momentum", "gram", "poly", "update", "apply", "ns_fused")
 
@@ -128,6 +128,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "muon_step_blocks": (i, [vp, ctypes.POINTER(Blocks), ctypes.POINTER(Hparams), vp]),
         "muon_ns_orthogonalize_blocks": (i, [vp, ctypes.POINTER(Blocks), f, vp]),
         "muon_expert_grad": (i, [vp, ctypes.POINTER(Experts), vp, ll, vp, ll, vp, ll, ll, i, f, f, vp]),
+        "muon_expert_grad_new": (i, [vp, ctypes.POINTER(Experts), vp, ll, vp, ll, vp, ll, ll, i, f, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -384,16 +385,25 @@ class Muon:
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             return [t if self._row_major(t) else t.contiguous() for t in tensors]
 
+    @staticmethod
+    def _new(like, shape, stream):
+        """Memory for a result of a call on `stream`."""
+        if stream is None:
+            return like.new_empty(shape)
+        import torch
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape)
+
     def expert_matmul(self, x, w, offsets, transpose=False, out=None, stream=None):
         """Products of sorted token rows with the weights of their experts.
 
         x: [tokens, cols]; w: [experts, rows, cols]; offsets: int32 CUDA [experts + 1], rows
         offsets[e] .. offsets[e+1]-1 of x belong to expert e.  Returns y [tokens, rows] with
         y[t] = w[e] @ x[t]; with ``transpose`` x is [tokens, rows] and y[t] = w[e].T @ x[t] (the
-        input gradient).  Rows of no expert are zero in a new result and left as they were in ``out``.
+        input gradient).  Rows of no expert are zero in a new result and left as they were in ``out``;
+        bad offsets (``status`` raises) leave no row to any expert.
         bf16 or fp32, any sizes; tensors whose rows are not contiguous are copied first.
         """
-        import torch
         if x.dim() != 2 or w.dim() != 3:
             raise ValueError("x must be 2-D and w 3-D")
         e, n, k = w.shape
@@ -407,11 +417,7 @@ class Muon:
             x, w = self._copied((x, w), stream)
         clear = out is None
         if clear:
-            if stream is None:
-                out = x.new_empty((tokens, n_out))
-            else:
-                with torch.cuda.stream(stream):
-                    out = x.new_empty((tokens, n_out))
+            out = self._new(x, (tokens, n_out), stream)
         else:
             self._on_device(out)
             if out.shape != (tokens, n_out) or out.dtype is not x.dtype or not self._row_major(out):
@@ -424,30 +430,42 @@ class Muon:
             self._check(st, "muon_expert_matmul")
         return out
 
-    def expert_grad(self, dy, x, offsets, out, beta=0.0, scale=1.0, stream=None):
+    def expert_grad(self, dy, x, offsets, out=None, beta=0.0, scale=1.0, stream=None):
         """out[e] = beta * out[e] + scale * dy_e.T @ x_e, the weight gradients of the experts.
 
         dy: [tokens, rows], x: [tokens, cols] (one dtype, rows sorted by expert as in expert_matmul);
         out: [experts, rows, cols], fp32 or the inputs' dtype, updated in place and returned.
-        beta=1 accumulates over micro-batches, beta=0 overwrites without reading.
+        beta=1 accumulates over micro-batches, beta=0 overwrites without reading.  Without out (beta=0)
+        the result is new, of the inputs' dtype.  Bad offsets (``status`` raises) leave out as it was
+        and a new result zero.
         """
-        if dy.dim() != 2 or x.dim() != 2 or out.dim() != 3:
+        if dy.dim() != 2 or x.dim() != 2 or (out is not None and out.dim() != 3):
             raise ValueError("dy and x must be 2-D and out 3-D")
-        e, n, k = out.shape
+        fresh = out is None
+        if fresh and beta != 0.0:
+            raise ValueError("beta: a new result has nothing to add to")
+        e, n, k = (max(offsets.numel() - 1, 0), dy.shape[1], x.shape[1]) if fresh else out.shape
         tokens = x.shape[0]
         if dy.shape != (tokens, n) or x.shape[1] != k or dy.dtype is not x.dtype:
             raise ValueError(f"dy, x: must be [tokens, {n}] and [tokens, {k}] of one dtype, got {tuple(dy.shape)} "
                              f"{dy.dtype} and {tuple(x.shape)} {x.dtype}")
-        if not self._row_major(out):
-            raise ValueError("out: the last dimension must be contiguous and nothing may overlap")
-        self._on_device(dy, x, out, offsets)
+        self._on_device(dy, x, offsets)
+        if not fresh:
+            if not self._row_major(out):
+                raise ValueError("out: the last dimension must be contiguous and nothing may overlap")
+            self._on_device(out)
         ex = self._experts(offsets, tokens, e, n, k, _dtype_code(x))
         if not (self._row_major(dy) and self._row_major(x)):
             dy, x = self._copied((dy, x), stream)
-        sg, ldg, _ = out.stride()
-        st = self.lib.muon_expert_grad(self.handle, ex, dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0),
-                                       out.data_ptr(), ldg, sg, _dtype_code(out), beta, scale,
-                                       self._device_stream(stream))
+        if fresh:
+            out = self._new(x, (e, n, k), stream)
+            st = self.lib.muon_expert_grad_new(self.handle, ex, dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0),
+                                               out.data_ptr(), k, n * k, ex.dtype, scale, self._device_stream(stream))
+        else:
+            sg, ldg, _ = out.stride()
+            st = self.lib.muon_expert_grad(self.handle, ex, dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0),
+                                           out.data_ptr(), ldg, sg, _dtype_code(out), beta, scale,
+                                           self._device_stream(stream))
         if st:
             self._check(st, "muon_expert_grad")
         return out

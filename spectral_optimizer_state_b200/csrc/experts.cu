@@ -200,11 +200,14 @@ __device__ __forceinline__ void zero_rows(uint32_t base, int chunks, int first, 
     for (int r = first + (lane >> 3); r < last; r += 4) st_shared_zero16(base + c * CHUNK_BYTES + r * 128 + (lane & 7) * 16);
 }
 
-// Rows the segments do not cover become zero: a warp of the grid takes a row at a time.
+// Output rows first .. last - 1 (STACK: of the gradients, counted through the experts) become zero: a warp of the
+// grid takes a row at a time.
+template <bool STACK>
 __device__ __forceinline__ void clear_rows(const ExpertParams& P, int first, int last, int warp, int warps, int lane) {
   const int bytes = P.out_f32 ? 4 : 2, row_bytes = P.features * bytes;
   for (int r = first + warp; r < last; r += warps) {
-    char* row = static_cast<char*>(P.out) + r * P.ld_out * bytes;
+    const int e = STACK ? r / P.rows : 0;
+    char* row = static_cast<char*>(P.out) + (STACK ? e * P.s_out + (r - e * P.rows) * P.ld_out : r * P.ld_out) * bytes;
     const int wide = P.vec ? row_bytes & ~15 : 0;
     for (int i = 16 * lane; i < wide; i += 512) *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
     for (int i = wide + 2 * lane; i < row_bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
@@ -815,10 +818,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __gri
       }
     }
     bulk_wait_group_all();
-    if (!B_MN && P.clear_rest && !*bad) {
+    if (P.clear_rest && (!B_MN || *bad)) {
       const int w = blockIdx.x * EPI_WARPS + warp - 2, warps = gridDim.x * EPI_WARPS;
-      clear_rows(P, 0, seg_off[0], w, warps, lane);
-      clear_rows(P, seg_off[P.experts], P.tokens, w, warps, lane);
+      if (B_MN) {
+        clear_rows<true>(P, 0, P.experts * P.rows, w, warps, lane);
+      } else {  // with bad offsets no row is of any segment
+        clear_rows<false>(P, 0, *bad ? P.tokens : seg_off[0], w, warps, lane);
+        if (!*bad) clear_rows<false>(P, seg_off[P.experts], P.tokens, w, warps, lane);
+      }
     }
   }
 

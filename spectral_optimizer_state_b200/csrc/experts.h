@@ -32,7 +32,7 @@ struct alignas(64) ExpertParams {
   long long ld_out, s_out;        // elements between rows / experts of the output
   int out_f32;
   int vec;                        // rows of the output start on 16-byte boundaries
-  int clear_rest;                 // products: zero the rows no segment covers
+  int clear_rest;                 // zero the rows no segment covers; gradient: all of it if the offsets are bad
   float beta, scale;              // weight gradient: out = beta out + scale acc
   int* status;
 };

@@ -1708,9 +1708,9 @@ muon_status muon_expert_matmul(muon_ctx* c, const muon_experts* ex, const void* 
                      Operand{X, 1, ex->tokens, in, 1, ldx, 0, 0}, p, static_cast<cudaStream_t>(stream));
 }
 
-muon_status muon_expert_grad(muon_ctx* c, const muon_experts* ex, const void* dY, long long ldy, const void* X,
-                             long long ldx, void* G, long long ldg, long long sg, int out_dtype, float beta,
-                             float scale, void* stream) {
+static muon_status expert_grad(muon_ctx* c, const muon_experts* ex, const void* dY, long long ldy, const void* X,
+                               long long ldx, void* G, long long ldg, long long sg, int out_dtype, float beta,
+                               float scale, bool fresh, void* stream) {
   const muon_status st = check_experts(c, ex);
   if (st != MUON_OK) return st;
   if (out_dtype != MUON_F32 && out_dtype != ex->dtype) return MUON_ERR_DTYPE;
@@ -1733,8 +1733,21 @@ muon_status muon_expert_grad(muon_ctx* c, const muon_experts* ex, const void* dY
           reinterpret_cast<uintptr_t>(G) % 16 == 0;
   p.beta = beta;
   p.scale = scale;
+  p.clear_rest = fresh;
   return run_experts(c, ex, EXPERT_WGRAD, Operand{X, 1, ex->tokens, ex->cols, 1, ldx, 0, 0},
                      Operand{dY, 1, ex->tokens, ex->rows, 1, ldy, 0, 0}, p, static_cast<cudaStream_t>(stream));
+}
+
+muon_status muon_expert_grad(muon_ctx* c, const muon_experts* ex, const void* dY, long long ldy, const void* X,
+                             long long ldx, void* G, long long ldg, long long sg, int out_dtype, float beta,
+                             float scale, void* stream) {
+  return expert_grad(c, ex, dY, ldy, X, ldx, G, ldg, sg, out_dtype, beta, scale, false, stream);
+}
+
+muon_status muon_expert_grad_new(muon_ctx* c, const muon_experts* ex, const void* dY, long long ldy, const void* X,
+                                 long long ldx, void* G, long long ldg, long long sg, int out_dtype, float scale,
+                                 void* stream) {
+  return expert_grad(c, ex, dY, ldy, X, ldx, G, ldg, sg, out_dtype, 0.f, scale, true, stream);
 }
 
 muon_status muon_step_blocks(muon_ctx* c, const muon_blocks* blocks, const muon_hparams* hp, void* stream) {

@@ -33,7 +33,7 @@ def _function():
                 if ctx.grad_into is not None:
                     ctx.muon.expert_grad(dy, x, offsets, ctx.grad_into, beta=1.0)
                 else:
-                    dw = ctx.muon.expert_grad(dy, x, offsets, torch.empty_like(w, memory_format=torch.contiguous_format))
+                    dw = ctx.muon.expert_grad(dy, x, offsets)
             return dx, dw, None, None, None
 
     return _ExpertLinear
@@ -44,7 +44,7 @@ def expert_linear(x, w, offsets, muon, grad_into=None):
 
     x: [tokens, cols], rows sorted by expert; w: [experts, rows, cols]; offsets: int32 CUDA
     [experts + 1] (rows offsets[e] .. offsets[e+1]-1 belong to expert e; rows of no expert give and
-    receive zeros); muon: the libmuon context whose scratch the products use.  bf16 or fp32.
+    receive zeros, and so does everything if the offsets are bad, which muon.status() reports); muon: the libmuon context whose scratch the products use.  bf16 or fp32.
     grad_into: an fp32 [experts, rows, cols] buffer that the weight gradient is added to, over as many
     backward passes as one likes; w.grad then stays None.
     """
