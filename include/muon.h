@@ -306,7 +306,9 @@ muon_status muon_adamw_step(void* const* W, const void* const* G, float* const* 
  * elements; the last dimension is contiguous.  Any sizes, strides and element alignments are taken:
  * bf16 operands whose rows do not start on 16-byte boundaries, and fp32 operands of calls with more than
  * 64 tokens an expert (and of larger gradients), are first repacked into context scratch.  bf16 operands
- * are multiplied with fp32 accumulation and rounded once; fp32 ones are split into three bf16 planes whose
+ * are multiplied with fp32 accumulation and rounded once (the tensor core's additions truncate: up to 2^-22
+ * of the sum for each 16 products; it sums at most 32768 elements, 512 for gradients into fp32, 128 for fp32
+ * operands, and such parts are added with rounding to nearest); fp32 ones are split into three bf16 planes whose
  * six leading products are accumulated in fp32 (fp32 infinities and values above 3.38e38 become NaN).
  * Offsets and sizes: 0 <= tokens <= 2^30, 1 <= rows, cols <= 32768, 1 <= experts <= MUON_MAX_EXPERTS.
  * Device-side status (a wait that ran out, bad offsets) is kept until muon_get_status reports it. */

@@ -65,6 +65,11 @@ constexpr uint32_t A_BYTES = FM * BK * 2;
 constexpr uint32_t CHUNK_BYTES = 64 * BK * 2;  // MN-major: 64 columns x 64 contraction rows
 // fp32 outputs: contraction tiles a TMEM accumulator sums before registers take over
 __host__ __device__ constexpr int part_tiles(int kind) { return kind >= F32_F32 ? 2 : 8; }
+// bf16 gradients: the same, for segments that are longer than this (32768 tokens), and the rows a tile of a launch
+// with such segments has at most, so that the sums fit the registers.  Sums of 8192 tokens would narrow the tiles
+// of ordinary launches (4 experts of 1536 x 768, 16384 tokens each: 155 us, 122 as it is); sums of 256 rows would
+// spill registers in all of them (64 of 512 x 512, 64 tokens each: 24.0 us, 21.3 as it is).
+constexpr int LONG_PART = 512, LONG_ROWS = 128;
 __host__ __device__ constexpr int epi_warps(int kind) { return kind == F32_SPLIT ? 4 : 8; }
 constexpr int SPLIT_WARPS = 8, SPLIT_ROWS = 64;  // F32_SPLIT: its warps, and rows of its tiles at most
 // Staging per epilogue warp: 32 rows x 32 bf16, or two boxes of 16 rows x 32 fp32.
@@ -408,14 +413,18 @@ __device__ __forceinline__ void issue_commit(uint32_t bar) {
   else tc_commit_elect(bar);
 }
 
-// OUT_F32: the accumulator is emptied into registers every PART_TILES contraction tiles, which keeps the
-// tensor core's own (truncating) fp32 additions few; bf16 outputs round far above that.
+// The tensor core's own fp32 additions truncate: one of 16 products loses up to two units of 2^-23 of the sum,
+// always towards zero.  So OUT_F32 empties the accumulator into registers every PART_TILES contraction tiles,
+// and gradients in bf16 every LONG_PART, as many elements as a product contracts at most: up to 4.9e-4 of the summed
+// magnitudes, against a rounding of up to 3.9e-3.  (One accumulator over 2^20 tokens of one sign lost 6.5e-3.)
 template <int MODE, int KIND, bool PAIR>
 __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __grid_constant__ ExpertParams P) {
   constexpr bool OUT_F32 = KIND != BF16_BF16;
   constexpr bool SPLIT = KIND == F32_SPLIT;
   static_assert(!(SPLIT && PAIR), "split tiles are of one CTA");
   constexpr int PLANES = KIND >= F32_F32 ? 3 : 1, SEGMENTS = KIND >= F32_F32 ? 6 : 1, PART_TILES = part_tiles(KIND);
+  constexpr bool PARTED = OUT_F32 || MODE == EXPERT_WGRAD;  // accumulators may hold parts of a contraction
+  constexpr int PART = OUT_F32 ? PART_TILES : LONG_PART;
   constexpr int THREADS = threads_of(KIND), EPI_WARPS = epi_warps(KIND);
   constexpr bool A_MN = MODE != EXPERT_FORWARD;
   constexpr bool B_MN = MODE == EXPERT_WGRAD;
@@ -509,7 +518,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __gri
       const int mine = PAIR ? rows / 2 : rows;
       // two stages have to fit (the narrowest width's always do)
       const bool fits = 2u * PLANES * (A_BYTES + b_bytes<B_MN, SPLIT>(mine)) <= ring_bytes(KIND) &&
-                        !(SPLIT && w > SPLIT_ROWS);
+                        !(SPLIT && w > SPLIT_ROWS) &&
+                        !(PARTED && !OUT_F32 && longest > LONG_PART * BK && w > LONG_ROWS);
       seg_cost[warp] = fits ? rounds * (static_cast<long long>(nk) * (FM + mine) + kTileOverhead) : LLONG_MAX;
       if (warp == 0) seg_longest = longest;
     }
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __gri
           tc_fence_after();
         }
         const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-        const int part_end = OUT_F32 ? min(kk + PART_TILES, nk) : nk;
+        const int part_end = PARTED ? min(kk + PART, nk) : nk;
         for (uint32_t more = 0; kk < part_end; ++kk, ring.next(stages)) {
           const int s = ring.s;
           ok = mbar_wait_bounded(full_bar(s), ring.phase, abort_flag, P.status);
@@ -759,14 +769,14 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __gri
       const int nk = B_MN ? (ti.kn + BK - 1) / BK : P.k_tiles;
       const long long at = (B_MN ? ti.e * P.s_out : 0ll) + static_cast<long long>(ti.r0) * P.ld_out + fw;
       const bool live = fw < P.features;
-      if (OUT_F32) {
-        constexpr int CHUNKS = SPLIT ? SPLIT_ROWS / 32 : 4, NEXT = 8 * EPI_WARPS;
+      if (OUT_F32 || (PARTED && nk > LONG_PART)) {
+        constexpr int CHUNKS = SPLIT ? SPLIT_ROWS / 32 : OUT_F32 ? 4 : LONG_ROWS / 64, NEXT = 8 * EPI_WARPS;
         float sum[CHUNKS][32];  // running sums of this warp's chunks
 #pragma unroll
         for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
-        for (int kk = 0; kk < nk; kk += PART_TILES) {
+        for (int kk = 0; kk < nk; kk += PART) {
           if (!take()) break;
 #pragma unroll
           for (int j = 0; j < CHUNKS; ++j) {
@@ -787,7 +797,10 @@ __global__ void __launch_bounds__(threads_of(KIND), 1) expert_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < CHUNKS; ++j) {
           const int c = 32 * half + NEXT * j;
-          if (live && c < ti.nr)
+          if (!live || c >= ti.nr) continue;
+          if (!OUT_F32)
+            add_column(P, at + lane + c * P.ld_out, fw + lane, min(32, ti.nr - c), sum[j]);
+          else
             store_rows(P, at + c * P.ld_out, ti.r0 + c, B_MN ? ti.e : 0, B_MN && ti.r0 + ti.nr == P.rows, stage, boxes, fw,
                        min(32, ti.nr - c), lane, sum[j]);
         }
