@@ -309,7 +309,8 @@ muon_status muon_adamw_step(void* const* W, const void* const* G, float* const* 
  * are multiplied with fp32 accumulation and rounded once (the tensor core's additions truncate: up to 2^-22
  * of the sum for each 16 products; it sums at most 32768 elements, 512 for gradients into fp32, 128 for fp32
  * operands, and such parts are added with rounding to nearest); fp32 ones are split into three bf16 planes whose
- * six leading products are accumulated in fp32 (fp32 infinities and values above 3.38e38 become NaN).
+ * six leading products are accumulated in fp32 (fp32 infinities and values above 3.38e38 become NaN; operands
+ * below 2^-110 are held to 2^-134, where the planes end).
  * Offsets and sizes: 0 <= tokens <= 2^30, 1 <= rows, cols <= 32768, 1 <= experts <= MUON_MAX_EXPERTS.
  * Device-side status (a wait that ran out, bad offsets) is kept until muon_get_status reports it. */
 typedef struct {
