@@ -46,6 +46,8 @@ def expert_linear(x, w, offsets, muon, grad_into=None):
     [experts + 1] (rows offsets[e] .. offsets[e+1]-1 belong to expert e; rows of no expert give and
     receive zeros, and so does everything if the offsets are bad, which muon.status() reports); muon: the libmuon context whose scratch the products use.  bf16 or fp32.
     grad_into: an fp32 [experts, rows, cols] buffer that the weight gradient is added to, over as many
-    backward passes as one likes; w.grad then stays None.
+    backward passes as one likes, if w requires a gradient.  w.grad then stays None, so an optimizer that
+    reads it passes w over: hand the buffer to ``MuonAdamW.step`` as w's gradient, or name it in
+    ``torch_optimizer(..., main_grads={name: buffer})``.
     """
     return _function().apply(x, w, offsets, muon, grad_into)

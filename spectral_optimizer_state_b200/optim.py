@@ -71,8 +71,20 @@ class MuonAdamW:
     def adamw_names(self):
         return [n for entries in self.adam.values() for (n, _, _, _) in entries]
 
+    @staticmethod
+    def _gradient(w, g, stream):
+        """g as the kernels read it: of w's dtype (rounded on `stream` if it is of another) and contiguous."""
+        if g.dtype == w.dtype and g.is_contiguous():
+            return g
+        if stream is None:
+            return g.to(w.dtype).contiguous()
+        import torch
+        with torch.cuda.stream(stream):
+            return g.to(w.dtype).contiguous()
+
     def step(self, grads, stream=None):
-        """grads: mapping name -> gradient tensor (same shape and dtype as the parameter).
+        """grads: mapping name -> gradient tensor of the parameter's shape.  One of another dtype (the fp32
+        buffer that micro-batches of bf16 weights were accumulated in) is rounded to the parameter's first.
 
         A parameter whose name is missing from ``grads`` or maps to None (frozen, or unused
         in this backward pass) is left untouched: its weights get no decay, its Muon momentum
@@ -81,7 +93,7 @@ class MuonAdamW:
         self.t += 1
         groups = []
         for key, entries in self.muon.items():
-            live = [(w, grads[n].contiguous(), mbuf) for n, w, mbuf in entries if grads.get(n) is not None]
+            live = [(w, self._gradient(w, grads[n], stream), mbuf) for n, w, mbuf in entries if grads.get(n) is not None]
             if len(key[0]) == 3:  # a stack: its matrices one by one
                 live = [t for w, g, mbuf in live for t in zip(w.unbind(0), g.unbind(0), mbuf.unbind(0))]
             for c0 in range(0, len(live), MAX_BATCH):
@@ -101,7 +113,7 @@ class MuonAdamW:
                 by_count.setdefault(self.adam_t[e[0]], []).append(e)
             for t, live in by_count.items():
                 W = [w.view(-1) for _, w, _, _ in live]
-                G = [grads[n].contiguous().view(-1) for n, _, _, _ in live]
+                G = [self._gradient(w, grads[n], stream).view(-1) for n, w, _, _ in live]
                 adamw_step(W, G, [m for _, _, m, _ in live], [v for _, _, _, v in live], t,
                            stream=stream, **self.adamw_hp)
 
@@ -131,17 +143,24 @@ class MuonAdamW:
         self.ctx.close()
 
 
-def torch_optimizer(named_params, mode="both", inner=None, **kw):
+def torch_optimizer(named_params, mode="both", inner=None, main_grads=None, **kw):
     """A ``torch.optim.Optimizer`` over MuonAdamW: ``step()`` reads each parameter's ``.grad``.
 
     named_params: (name, parameter) pairs, e.g. ``model.named_parameters()``.  Parameters whose
     ``.grad`` is None at ``step()`` are skipped, as ``torch.optim.AdamW`` skips them: no decay,
-    no momentum step, no moment update.  ``inner`` replaces the MuonAdamW instance (host-side
+    no momentum step, no moment update.  ``main_grads`` ({name: buffer}) names the parameters whose
+    gradients are accumulated elsewhere (``expert_linear(..., grad_into=buffer)``, which leaves ``.grad``
+    None): ``step()`` reads their buffers and ``zero_grad()`` clears them.  ``inner`` replaces the MuonAdamW instance (host-side
     tests only).
     """
     import torch
 
     named = [(n, p) for n, p in named_params]
+    buffers = dict(main_grads or {})
+    shapes = {n: p.shape for n, p in named}
+    for n, b in buffers.items():
+        if n not in shapes or b.shape != shapes[n]:
+            raise ValueError(f"main_grads: {n} is no parameter of shape {tuple(b.shape)}")
 
     class MuonAdamWOptimizer(torch.optim.Optimizer):
         def __init__(self):
@@ -155,9 +174,17 @@ def torch_optimizer(named_params, mode="both", inner=None, **kw):
             if closure is not None:
                 with torch.enable_grad():
                     loss = closure()
-            grads = {n: p.grad for n, p in named}
+            for n, p in named:
+                if n in buffers and p.grad is not None:
+                    raise ValueError(f"{n} has both a gradient and an accumulation buffer")
+            grads = {n: buffers.get(n, p.grad) for n, p in named}
             self.inner.step(grads)
             return loss
+
+        def zero_grad(self, set_to_none=True):
+            super().zero_grad(set_to_none)
+            for b in buffers.values():
+                b.zero_()
 
         def state_dict(self):
             return self.inner.state_dict()
