@@ -353,8 +353,8 @@ muon_status muon_expert_grad_new(muon_ctx* ctx, const muon_experts* ex, const vo
  * >= cols), so that the matrices may be views of larger ones; none of W or M may overlap another (the same
  * one twice is refused with MUON_ERR_INVALID_ARG).  The shape scale is that of each
  * block's own rows and columns.
- * Limits: the shorter side of a block is at most 128; the longer one at most 4096 (bf16) or 2048
- * (fp32), more for shorter sides below 113, else MUON_ERR_UNSUPPORTED_SHAPE.
+ * Limits: the shorter side of a block is at most 128; the longer one at most 5632 (bf16) or 2560
+ * (fp32), more for many shorter sides below 113 (muon_check_blocks tells), else MUON_ERR_UNSUPPORTED_SHAPE.
  * The iterates are held in fp16 (fp32 blocks: two fp16 planes, 22 bits) with fp32 accumulation, scaled
  * by a power of two chosen from the coefficient table; a table whose iterates could pass 2^15 from
  * singular values of at most 1 is refused with MUON_ERR_INVALID_ARG.
@@ -370,6 +370,10 @@ typedef struct {
   int block_rows, block_cols;
   int dtype;             /* muon_dtype of W and G                                        */
 } muon_blocks;
+
+/* Whether the block calls take blocks of block_rows x block_cols of rows x cols matrices of `dtype`: MUON_OK, or
+ * the error they return for these sizes.  Looks at sizes alone; needs no context and no GPU. */
+muon_status muon_check_blocks(int rows, int cols, int block_rows, int block_cols, int dtype);
 
 /* The Muon step of muon_step on every block. */
 muon_status muon_step_blocks(muon_ctx* ctx, const muon_blocks* blocks, const muon_hparams* hp, void* stream);

@@ -8,7 +8,6 @@ call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Iterable, Sequence
@@ -39,7 +38,7 @@ EXPORTS = (
     "muon_ns_orthogonalize", "muon_get_status", "muon_get_norms", "muon_workspace_bytes",
     "muon_profile_enable", "muon_profile_read", "muon_momentum_norm_noalloc", "muon_adamw_step",
     "muon_power_iteration", "muon_min_singular", "muon_step_capped", "muon_expert_matmul", "muon_expert_grad",
-    "muon_expert_grad_new", "muon_step_blocks", "muon_ns_orthogonalize_blocks",
+    "muon_expert_grad_new", "muon_check_blocks", "muon_step_blocks", "muon_ns_orthogonalize_blocks",
 )
 KERNEL_KINDS = ("momentum", "gram", "poly", "update", "apply", "ns_fused")
 
@@ -125,6 +124,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "muon_min_singular": (i, [vp, pvp, pvp, vp, vp, i, i, i, i, i, vp]),
         "muon_step_capped": (i, [vp, pvp, pvp, pvp, pvp, pvp, i, i, i, i, ctypes.POINTER(Hparams), vp, vp]),
         "muon_expert_matmul": (i, [vp, ctypes.POINTER(Experts), vp, ll, vp, ll, ll, vp, ll, i, i, vp]),
+        "muon_check_blocks": (i, [i, i, i, i, i]),
         "muon_step_blocks": (i, [vp, ctypes.POINTER(Blocks), ctypes.POINTER(Hparams), vp]),
         "muon_ns_orthogonalize_blocks": (i, [vp, ctypes.POINTER(Blocks), f, vp]),
         "muon_expert_grad": (i, [vp, ctypes.POINTER(Experts), vp, ll, vp, ll, vp, ll, ll, i, f, f, vp]),
@@ -141,6 +141,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
 
 def _ptrs(tensors: Sequence) -> ctypes.Array:
     return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+def check_block(shape, block, dtype):
+    """Refuses (MuonError) a `block` = (rows, columns; None: the whole side) that step_blocks cannot take of matrices
+    of this shape and dtype; needs no GPU."""
+    import torch
+    side = [int(n) for n in shape]
+    br, bc = (side[i] if block[i] is None else min(int(block[i]), side[i]) for i in range(2))
+    code = _dtype_code(torch.empty(0, dtype=dtype))
+    st = load_library().muon_check_blocks(*(min(n, 2 ** 31 - 1) for n in side), max(br, 0), max(bc, 0), code)
+    if st:
+        raise MuonError(st, f"blocks of {br} x {bc} of {side[0]} x {side[1]} {dtype} matrices")
 
 
 def _dtype_code(t) -> int:
@@ -506,7 +518,7 @@ class Muon:
 
         W, G, M: lists of same-shape 2-D tensors (or 3-D stacks) as in ``step``; rows contiguous, any
         row stride, so views of larger weights may be stepped.  The shorter side of a block is at
-        most 128.  Up to MAX_BATCH matrices a call, none of which may overlap another.
+        most 128, the longer one at most 5632 (bf16) or 2560 (fp32), or more (``check_block``).  Up to MAX_BATCH matrices a call, none of which may overlap another.
         """
         b = self._blocks(W, G, M, block)
         h = self.hparams(**hp)

@@ -11,6 +11,7 @@ namespace muon {
 // The short side of a block is at most this.
 constexpr int kBlockMaxShort = 128;
 constexpr int kBlockMaxCluster = 8;
+constexpr int kBlockMost = 1 << 27;  // blocks of a call
 
 struct BlockParams {
   void* w[MUON_MAX_BATCH];        // W (updated), or Out

@@ -996,50 +996,53 @@ double table_bound(const float* abc, int k) {
   return most;
 }
 
-muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* hp, bool step, float eps,
-                       cudaStream_t s) {
-  if (!c || !bl || !bl->W || !bl->G || (step && !bl->M)) return MUON_ERR_INVALID_ARG;
-  if (bl->dtype != MUON_BF16 && bl->dtype != MUON_F32) return MUON_ERR_DTYPE;
-  if (bl->batch < 1 || bl->batch > MUON_MAX_BATCH || bl->rows < 1 || bl->cols < 1 || bl->block_rows < 1 ||
-      bl->block_cols < 1)
-    return MUON_ERR_INVALID_ARG;
-  if (bl->rows > 32768 || bl->cols > 32768) return MUON_ERR_UNSUPPORTED_SHAPE;
-  if (bl->rows > 1 && (bl->ldw < bl->cols || bl->ldg < bl->cols || (step && bl->ldm < bl->cols)))
-    return MUON_ERR_INVALID_ARG;
-  const bool f32 = bl->dtype == MUON_F32;
-  BlockParams p;
-  std::memset(static_cast<void*>(&p), 0, sizeof(p));
-  p.block_rows = std::min(bl->block_rows, bl->rows);
-  p.block_cols = std::min(bl->block_cols, bl->cols);
-  p.rows = bl->rows;
-  p.cols = bl->cols;
-  p.ldw = bl->ldw;
-  p.ldg = bl->ldg;
-  p.ldm = bl->ldm;
-  p.grid_cols = (p.cols + p.block_cols - 1) / p.block_cols;
-  p.per_matrix = p.grid_cols * ((p.rows + p.block_rows - 1) / p.block_rows);
-  const long long total = static_cast<long long>(p.per_matrix) * bl->batch;
-  const bool tall = p.block_rows > p.block_cols;
+constexpr size_t kBlockMostSmem = 226 * 1024;
+
+// How matrices of rows x cols are cut: sizes, grid, the cluster that holds a block and the shared memory each
+// of its CTAs needs.
+muon_status plan_blocks(int rows, int cols, int block_rows, int block_cols, int dtype, BlockParams& p, size_t* smem) {
+  if (dtype != MUON_BF16 && dtype != MUON_F32) return MUON_ERR_DTYPE;
+  if (rows < 1 || cols < 1 || block_rows < 1 || block_cols < 1) return MUON_ERR_INVALID_ARG;
+  if (rows > 32768 || cols > 32768) return MUON_ERR_UNSUPPORTED_SHAPE;
+  p.block_rows = std::min(block_rows, rows);
+  p.block_cols = std::min(block_cols, cols);
+  p.rows = rows;
+  p.cols = cols;
+  p.grid_cols = (cols + p.block_cols - 1) / p.block_cols;
+  p.per_matrix = p.grid_cols * ((rows + p.block_rows - 1) / p.block_rows);
   const int m = std::min(p.block_rows, p.block_cols), n = std::max(p.block_rows, p.block_cols);
-  if (m > kBlockMaxShort || total > (1 << 27)) return MUON_ERR_UNSUPPORTED_SHAPE;
+  if (m > kBlockMaxShort || p.per_matrix > kBlockMost) return MUON_ERR_UNSUPPORTED_SHAPE;
   // Clusters: the fewest CTAs whose shared memory holds the block (blocks of 2048 x 128 in bf16: four CTAs
   // 1767 us, five 2330, eight 3130: an SM holds one CTA of a cluster, and the exchange of the Gram partials
   // does not shrink).  Where eight do not, the exchange takes the place of A, at two barriers more each (with
   // them three CTAs hold that block too, in 1870 us).
-  constexpr size_t kMostSmem = 226 * 1024, kTwoPerSm = (228 * 1024) / 2 - 1024, kNoThird = 77 * 1024,
-                   kAlone = 152 * 1024;
-  size_t smem = 0;
-  for (int i = 1; i <= kBlockMaxCluster + 1 && smem == 0; ++i) {
-    const int cl = std::min(i, kBlockMaxCluster), slice = round64((n + cl - 1) / cl);
-    const bool alias = i > kBlockMaxCluster;
-    const size_t bytes = block_smem_bytes(m, slice, tall, f32, cl, alias);
-    if (bytes > kMostSmem) continue;
-    p.cluster = cl;
-    p.slice = slice;
-    p.alias = alias;
-    smem = bytes;
+  for (int i = 1; i <= kBlockMaxCluster + 1; ++i) {
+    p.cluster = std::min(i, kBlockMaxCluster);
+    p.slice = round64((n + p.cluster - 1) / p.cluster);
+    p.alias = i > kBlockMaxCluster;
+    *smem = block_smem_bytes(m, p.slice, p.block_rows > p.block_cols, dtype == MUON_F32, p.cluster, p.alias);
+    if (*smem <= kBlockMostSmem) return MUON_OK;
   }
-  if (smem == 0) return MUON_ERR_UNSUPPORTED_SHAPE;
+  return MUON_ERR_UNSUPPORTED_SHAPE;
+}
+
+muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* hp, bool step, float eps,
+                       cudaStream_t s) {
+  if (!c || !bl || !bl->W || !bl->G || (step && !bl->M)) return MUON_ERR_INVALID_ARG;
+  if (bl->batch < 1 || bl->batch > MUON_MAX_BATCH) return MUON_ERR_INVALID_ARG;
+  BlockParams p;
+  std::memset(static_cast<void*>(&p), 0, sizeof(p));
+  size_t smem = 0;
+  const muon_status planned = plan_blocks(bl->rows, bl->cols, bl->block_rows, bl->block_cols, bl->dtype, p, &smem);
+  if (planned != MUON_OK) return planned;
+  if (bl->rows > 1 && (bl->ldw < bl->cols || bl->ldg < bl->cols || (step && bl->ldm < bl->cols)))
+    return MUON_ERR_INVALID_ARG;
+  const bool f32 = bl->dtype == MUON_F32, tall = p.block_rows > p.block_cols;
+  p.ldw = bl->ldw;
+  p.ldg = bl->ldg;
+  p.ldm = bl->ldm;
+  const long long total = static_cast<long long>(p.per_matrix) * bl->batch;
+  if (total > kBlockMost) return MUON_ERR_UNSUPPORTED_SHAPE;
   // TMEM is shared by the SM's CTAs: never more than 512 columns between those of this library that fit
   // beside one another (of any launch: two calls may run at once), so that no CTA waits for columns
   // while its cluster waits for it.  Every kernel with TMEM takes at least 77 KB, those with all of it
@@ -1048,6 +1051,7 @@ muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* h
   // and 175) and asks L2 for the block that follows while it multiplies (768 blocks of 2048 x 128: 1769 us, 1838
   // without); where two share an SM, one loads while the other multiplies, more threads cost 186 instead of
   // 153 us and the request changes nothing (148.2 and 148.5).
+  constexpr size_t kTwoPerSm = (228 * 1024) / 2 - 1024, kNoThird = 77 * 1024, kAlone = 152 * 1024;
   const bool alone = smem > kTwoPerSm || p.cluster > 1;
   p.tmem_cols = alone ? 512 : 256;
   p.threads = alone ? 512 : 256;
@@ -1748,6 +1752,12 @@ muon_status muon_expert_grad_new(muon_ctx* c, const muon_experts* ex, const void
                                  long long ldx, void* G, long long ldg, long long sg, int out_dtype, float scale,
                                  void* stream) {
   return expert_grad(c, ex, dY, ldy, X, ldx, G, ldg, sg, out_dtype, 0.f, scale, true, stream);
+}
+
+muon_status muon_check_blocks(int rows, int cols, int block_rows, int block_cols, int dtype) {
+  BlockParams p;
+  size_t smem = 0;
+  return plan_blocks(rows, cols, block_rows, block_cols, dtype, p, &smem);
 }
 
 muon_status muon_step_blocks(muon_ctx* c, const muon_blocks* blocks, const muon_hparams* hp, void* stream) {

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 from collections import OrderedDict
 
-from .binding import MAX_BATCH, MAX_GROUPS, Muon, adamw_step
+from .binding import MAX_BATCH, MAX_GROUPS, Muon, adamw_step, check_block
 
 
 def takes_muon(name: str, shape, mode: str = "both", stacked: bool = False) -> bool:
@@ -36,7 +36,8 @@ class MuonAdamW:
     matrices (experts x rows x cols); every matrix is stepped on its own.
     blocks: {part of a name: (block rows, block cols)}; a selected parameter whose name contains the
     part is stepped block by block (``Muon.step_blocks``: heads of a projection, small experts), the
-    first match counting.  None in place of a size means the whole side.
+    first match counting.  None in place of a size means the whole side.  A block that ``Muon.step_blocks``
+    does not take is refused here.
     """
 
     def __init__(self, named_params, mode="both", device=0, coeffs=None,
@@ -47,15 +48,21 @@ class MuonAdamW:
         self.muon_hp.update(muon_hp or {})
         self.adamw_hp = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
         self.adamw_hp.update(adamw_hp or {})
+        named_params = [(name, p) for name, p in named_params]
+        cut = {}  # name -> block of the parameters that are stepped block by block
+        for name, p in named_params:
+            block = next((tuple(b) for part, b in (blocks or {}).items() if part in name), None)
+            if block is not None and takes_muon(name, tuple(p.shape), mode, stacked):
+                check_block(p.shape[-2:], block, p.dtype)
+                cut[name] = block
         self.ctx = Muon(device, coeffs)
         self.muon = OrderedDict()   # (shape, dtype[, block]) -> [(name, W, M)]
         self.adam = OrderedDict()   # dtype -> [(name, W, m, v)]
         for name, p in named_params:
             if takes_muon(name, tuple(p.shape), mode, stacked):
                 key = (tuple(p.shape), p.dtype)
-                block = next((tuple(b) for part, b in (blocks or {}).items() if part in name), None)
-                if block is not None:
-                    key += (block,)
+                if name in cut:
+                    key += (cut[name],)
                 self.muon.setdefault(key, []).append((name, p, torch.zeros(p.shape, dtype=torch.float32, device=p.device)))
             else:
                 z = lambda: torch.zeros(p.numel(), dtype=torch.float32, device=p.device)  # noqa: E731
