@@ -147,12 +147,24 @@ def check_block(shape, block, dtype):
     """Refuses (MuonError) a `block` = (rows, columns; None: the whole side) that step_blocks cannot take of matrices
     of this shape and dtype; needs no GPU."""
     import torch
-    side = [int(n) for n in shape]
-    br, bc = (side[i] if block[i] is None else min(int(block[i]), side[i]) for i in range(2))
-    code = _dtype_code(torch.empty(0, dtype=dtype))
-    st = load_library().muon_check_blocks(*(min(n, 2 ** 31 - 1) for n in side), max(br, 0), max(bc, 0), code)
+    rows, cols, br, bc = _block_sizes(shape, block)
+    st = load_library().muon_check_blocks(rows, cols, br, bc, _dtype_code(torch.empty(0, dtype=dtype)))
     if st:
-        raise MuonError(st, f"blocks of {br} x {bc} of {side[0]} x {side[1]} {dtype} matrices")
+        raise MuonError(st, f"blocks of {br} x {bc} of {rows} x {cols} {dtype} matrices")
+
+
+def _fits_int(*sizes):
+    """The library's sizes are 32-bit; what does not fit is refused as it refuses what is too large."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise MuonError(2, f"sizes {sizes}")
+
+
+def _block_sizes(shape, block):
+    """(rows, cols, block rows, block cols) for the library: None and more than the side are the whole side."""
+    rows, cols = int(shape[0]), int(shape[1])
+    _fits_int(rows, cols)
+    br, bc = (side if b is None else max(min(int(b), side), 0) for b, side in zip(block, (rows, cols)))
+    return rows, cols, br, bc
 
 
 def _dtype_code(t) -> int:
@@ -375,6 +387,7 @@ class Muon:
         if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous():
             raise ValueError(f"offsets: must be {experts + 1} contiguous int32, got {tuple(offsets.shape)} "
                              f"{offsets.dtype}")
+        _fits_int(tokens, experts, rows, cols)
         return Experts(offsets.data_ptr(), experts, tokens, rows, cols, dtype)
 
     def _on_device(self, *tensors):
@@ -506,11 +519,11 @@ class Muon:
             raise ValueError("matrices must be 2-D")
         if len(W) != len(G) or (M is not None and len(W) != len(M)):
             raise ValueError("the lists must have the same length")
-        br, bc = (shape[i] if block[i] is None else int(block[i]) for i in range(2))
+        rows, cols, br, bc = _block_sizes(shape, block)
         ldw, ldg = self._strided(W, shape, dt, "W"), self._strided(G, shape, dt, "G")
         ldm = self._strided(M, shape, torch.float32, "M") if M is not None else 0
         pw, pg, pm = _ptrs(W), _ptrs(G), _ptrs(M) if M is not None else None
-        return Blocks(pw, pg, pm, ldw, ldg, ldm, len(W), shape[0], shape[1], br, bc, _dtype_code(W[0]))
+        return Blocks(pw, pg, pm, ldw, ldg, ldm, len(W), rows, cols, br, bc, _dtype_code(W[0]))
 
     def step_blocks(self, W, G, M, block, stream=None, **hp):
         """One Muon step in which every `block` = (rows, columns) of each matrix is its own: normalised,
