@@ -350,9 +350,9 @@ muon_status muon_expert_grad_new(muon_ctx* ctx, const muon_experts* ex, const vo
  * the pages do not say how finely a fused projection is cut.)
  * One launch per call: a block stays in shared memory from its norm to its apply.
  * W, G, M: host arrays of `batch` device pointers as in muon_group, with row strides ld* (elements,
- * >= cols), so that the matrices may be views of larger ones; none of W or M may overlap another (the same
- * one twice is refused with MUON_ERR_INVALID_ARG).  The shape scale is that of each
- * block's own rows and columns.
+ * >= cols), so that the matrices may be views of larger ones; none of W or M may overlap another, nor a G but
+ * that G may be its own W with the same stride (an address given where it may not be is refused with
+ * MUON_ERR_INVALID_ARG).  The shape scale is that of each block's own rows and columns.
  * Limits: the shorter side of a block is at most 128; the longer one at most 5632 (bf16) or 2560
  * (fp32), more for many shorter sides below 113 (muon_check_blocks tells), else MUON_ERR_UNSUPPORTED_SHAPE.
  * The iterates are held in fp16 (fp32 blocks: two fp16 planes, 22 bits) with fp32 accumulation, scaled
@@ -378,7 +378,7 @@ muon_status muon_check_blocks(int rows, int cols, int block_rows, int block_cols
 /* The Muon step of muon_step on every block. */
 muon_status muon_step_blocks(muon_ctx* ctx, const muon_blocks* blocks, const muon_hparams* hp, void* stream);
 
-/* W_block = NS_k(G_block / (||G_block||_F + eps)) for every block; W may be G with the same stride. */
+/* W_block = NS_k(G_block / (||G_block||_F + eps)) for every block. */
 muon_status muon_ns_orthogonalize_blocks(muon_ctx* ctx, const muon_blocks* blocks, float eps, void* stream);
 
 /* Bytes of the library's static device scratch used by muon_momentum_norm_noalloc. */

@@ -542,7 +542,7 @@ class Muon:
     def orthogonalize_blocks(self, X, Out, block, eps=1e-7, stream=None):
         """Out[l] = NS_k of every `block` of X[l] on its own, each divided by its norm + eps first.
 
-        Lists or stacks as in ``step_blocks``; Out may be X.  A block whose norm is not finite leaves
+        Lists or stacks as in ``step_blocks``; Out[l] may be X[l].  A block whose norm is not finite leaves
         its part of Out as it was.
         """
         b = self._blocks(Out, X, None, block)

@@ -1071,14 +1071,16 @@ muon_status run_blocks(muon_ctx* c, const muon_blocks* bl, const muon_hparams* h
     const uintptr_t wg = reinterpret_cast<uintptr_t>(p.w[l]) | reinterpret_cast<uintptr_t>(p.g[l]);
     if (wg % (8 * eb) || reinterpret_cast<uintptr_t>(p.m[l]) % 32) p.vec = 0;
   }
-  // a matrix given twice would be stepped twice at the same time
-  auto repeated = [&](const void* const* list) {
-    const void* sorted[MUON_MAX_BATCH];
-    std::copy(list, list + bl->batch, sorted);
-    std::sort(sorted, sorted + bl->batch);
-    return std::adjacent_find(sorted, sorted + bl->batch) != sorted + bl->batch;
-  };
-  if (repeated(bl->W) || (step && repeated(reinterpret_cast<const void* const*>(bl->M)))) return MUON_ERR_INVALID_ARG;
+  // What is written may be given once, or a matrix would be stepped twice at the same time; what is read may not be
+  // written by another block at that time: G may be its own W, lying the same way, and no other W nor any M.
+  const void* written[2 * MUON_MAX_BATCH];
+  const void** end = std::copy(p.w, p.w + bl->batch, written);
+  if (step) end = std::copy(p.m, p.m + bl->batch, end);
+  std::sort(written, end);
+  if (std::adjacent_find(written, end) != end) return MUON_ERR_INVALID_ARG;
+  for (int l = 0; l < bl->batch; ++l)
+    if (p.g[l] == p.w[l] ? bl->rows > 1 && bl->ldg != bl->ldw : std::binary_search(written, end, p.g[l]))
+      return MUON_ERR_INVALID_ARG;
   const double bound = table_bound(c->coeffs, c->k);
   if (!(bound < 32768.0)) return MUON_ERR_INVALID_ARG;
   p.store_scale = static_cast<float>(std::ldexp(1.0, std::min(12, static_cast<int>(std::floor(std::log2(32768.0 / bound))))));
