@@ -498,8 +498,6 @@ class Muon:
     # -------------------------------------------------------------- blocks
     def _strided(self, ts, shape, dtype, what):
         """Row stride of a list of same-shape 2-D tensors (or of a 3-D stack) with contiguous rows."""
-        if len(ts) == 0:
-            raise ValueError(f"{what}: empty list")
         ld = ts[0].stride(0)
         for t in ts:
             if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
@@ -514,6 +512,8 @@ class Muon:
 
     def _blocks(self, W, G, M, block):
         import torch
+        if len(W) == 0:
+            raise ValueError("W: empty list")
         shape, dt = tuple(W[0].shape), W[0].dtype
         if len(shape) != 2:
             raise ValueError("matrices must be 2-D")

@@ -62,3 +62,12 @@ def test_block_sizes_beyond_32_bits(host, monkeypatch, block, want):
     host.orthogonalize_blocks([torch.zeros(6, 8)], [torch.zeros(6, 8)], block)
     b = host.lib.calls[0][1][1]._obj
     assert (b.block_rows, b.block_cols) == want
+
+
+def test_no_matrices_are_refused_like_other_bad_lists(host):
+    for W in ([], torch.zeros(0, 6, 8)):
+        with pytest.raises(ValueError):
+            host.orthogonalize_blocks(W, W, (3, 8))
+        with pytest.raises(ValueError):
+            host.block_step_plan(W, W, W, (3, 8))
+    assert host.lib.calls == []
