@@ -97,19 +97,10 @@ __device__ __forceinline__ uint32_t instr_desc_f16(int mrows, int n, bool a_mn, 
          (static_cast<uint32_t>(mrows >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
+// The barrier's arrival is for converged warps.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t out;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
-  return out;
+  cluster_sync_all();
 }
 __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
   double v;
@@ -560,7 +551,7 @@ __device__ __forceinline__ void send_item(uint32_t as, int a_rows, uint32_t a_pl
   split8<PLANES>(v, o);
   const uint32_t dst = piece_at(as, a_rows, row, col);
   for (int r = 0; r < C; ++r) {
-    const uint32_t to = map_rank(dst, r);
+    const uint32_t to = map_shared_rank(dst, r);
 #pragma unroll
     for (int q = 0; q < PLANES; ++q) st_cluster_v4(to + q * a_plane, o[q]);
   }
@@ -592,7 +583,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) block_kernel(const __grid_cons
 
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int C = CLUSTER ? P.cluster : 1;
-  const uint32_t rank = CLUSTER ? cluster_rank() : 0u;
+  const uint32_t rank = CLUSTER ? cluster_cta_rank() : 0u;
   const int b = static_cast<int>(blockIdx.x) / C;
   const int l = b / P.per_matrix, in_mat = b - l * P.per_matrix;
   const int bi = in_mat / P.grid_cols, bj = in_mat - bi * P.grid_cols;
@@ -676,7 +667,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) block_kernel(const __grid_cons
     if (tid == 0) V.sum = total;
     cluster_sync();
     total = 0.0;
-    for (int r = 0; r < C; ++r) total += ld_cluster_f64(map_rank(smem_addr(&V.sum), r));
+    for (int r = 0; r < C; ++r) total += ld_cluster_f64(map_shared_rank(smem_addr(&V.sum), r));
   }
   const float nu = static_cast<float>(sqrt(total));
   const float inv = 1.f / (nu + P.eps);
@@ -820,7 +811,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) block_kernel(const __grid_cons
             load_gram<F32>(tmem + lane_off + 32 * tc, mp, sets, r);
             if (amine) {
               const int k = 2 * (tr * side - tr * (tr - 1) / 2 + tc - tr) + ((arow >> 4) & 1), slot = k / C;
-              const uint32_t to = map_rank(buf + (rank * share + slot) * 2048 + (arow & 15) * 16, k - slot * C);
+              const uint32_t to = map_shared_rank(buf + (rank * share + slot) * 2048 + (arow & 15) * 16, k - slot * C);
 #pragma unroll
               for (int h = 0; h < 8; ++h)
                 st_cluster_v4(to + 256 * h, np > 0 ? make_uint4(r[4 * h], r[4 * h + 1], r[4 * h + 2], r[4 * h + 3])
@@ -924,7 +915,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) block_kernel(const __grid_cons
     bool good = *abort_flag == 0;
     if (CLUSTER) {
       cluster_sync();
-      for (int r = 0; r < C; ++r) good = good && __float_as_int(ld_cluster_f(map_rank(smem_addr(&V.abort), r))) == 0;
+      for (int r = 0; r < C; ++r) good = good && __float_as_int(ld_cluster_f(map_shared_rank(smem_addr(&V.abort), r))) == 0;
     }
     if (good) {
       float lrs = P.lr;
