@@ -27,9 +27,11 @@
 // Measured (GPU time; floor: the bytes at the copy rate of 6.53 TB/s or the operations at the library's
 // 1.62 PFLOP/s) and what bounds it:
 //   32 experts of 4096 x 2048, 32768 tokens   430 us (339: operations)  tensor pipe, 77 % busy; 5.8 GB through L2
-//   8 of 1536 x 768, 8192 tokens              22.8 us (11.9: operations)  two rounds of tiles, their start and end
+//     (up to a hundred in a row, at 1965 MHz; a thousand run at 1.36 GHz under the power cap and take 482)
+//   8 of 1536 x 768, 8192 tokens              22.8 us (11.9: operations)  210 pair tiles or more for 74 pairs: three
+//     rounds, 14 us of products, and the start of the first and the draining of the last
 //   64 of 1536 x 768, 24 tokens               14.0 us (8.7: bytes)  set-up 2.4 us, first loads 1.8, last stores 2
-//   input gradient, 16 of them, 8191 tokens   25.0 us (11.9)  as above, segments uneven
+//   input gradient, 16 of them, 8191 tokens   25.0 us (11.9)  about 132 pair tiles: two rounds, the second 80 % full
 //   gradient into fp32, 16 of them            48.5 us (28.9: bytes)  additions in the memory system, 2 TB/s of them
 // A launch sets up while the one before it drains (programmatic serialisation): 14.0 instead of 14.5 us for
 // the fourth, 22.8 instead of 23.7 us for the second.

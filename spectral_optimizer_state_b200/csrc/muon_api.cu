@@ -862,12 +862,18 @@ bool stack_ok(const void* p, long long ld, long long s, int mats, int rows, int 
 }
 
 // Whether two CTAs share each tile (256 features).  A pair loads a third less per product but starts
-// slower and rounds features up to 256.  Measured with 16 experts (us, single -> pair): bf16 products of
-// 2048 x 2048 weights, 64 tokens an expert 32.4 -> 34.3, 256 tokens 42.6 -> 39.7, 1024 tokens 112 -> 103;
-// 640 columns 27.5 -> 28.9 (a sixth of the pairs' features idle).  bf16 gradients of 1536 x 768, 256
-// tokens 29.2 -> 29.9, 1024 tokens 56.0 -> 49.8.  fp32 loads three planes of everything, so pairs pay
-// earlier: 640 x 768, 64 tokens 34.6 -> 36.5, 128 tokens 48.5 -> 42.3; gradients of 384 x 768, 16 tokens
-// 21.5 -> 20.2, of 256 x 768 19.5 -> 19.6.
+// slower and rounds features up to 256.  Measured with 16 experts (us, single -> pair); where the two cross
+// depends on how tiles fill the last round, and the limits lie between the crossings:
+//   bf16 products, millions of outputs: 2048 x 2048 weights 4.2: 31.5 -> 33.6, 5.2: 35.4 -> 34.3, 6.0: 36.1 -> 34.5,
+//     8.4: 40 -> 37.8; 1536 x 768 4.7: 18.2 -> 18.9, 5.9: 19.1 -> 19.2, 7.9: 21.8 -> 22.5, 12.6: 24.9 -> 23.6, with
+//     8 experts 6.1: 15.9 -> 17.2, 9.4: 17.4 -> 17.9; their input gradients 3.1: 17.5 -> 17.4, 4.7: 20 -> 23.5, 5.9:
+//     24.9 -> 24.2, 7.9: 28.3 -> 25.7.  640 columns, a sixth of the pairs' features idle: 27.5 -> 28.9.
+//   bf16 gradients, tokens an expert: 1536 x 768 384: 40.1 -> 41.6, 448: 42.0 -> 40.7, 496: 45.0 -> 41.7, 768: 51 -> 48;
+//     2048 x 2048, 8 experts 384: 64.6 -> 66.5, 512: 71 -> 65.
+//   fp32 loads three planes of everything, so pairs pay earlier.  Products, millions of outputs: 640 x 768 0.66:
+//     33.5 -> 35.2, 0.98: 43.7 -> 37.4, 1.3: 46.7 -> 39.8, 1.6: 46.8 -> 48.5; 1536 x 768 1.2: 70.4 -> 72.4, 1.6: 71.5 ->
+//     73.3, 2.4: 81.4 -> 75.4.  Gradients: 16 tokens 3.1: 17.4 -> 17.6, 3.9: 19.3 -> 18.2, 4.7: 19.8 -> 18.2, 6.3: 24 ->
+//     20.8; 128 tokens 3.1: 20.4 -> 20.0, 4.3: 24 -> 20.7.
 bool expert_pair(ExpertMode mode, bool f32, long long features, long long rows, long long tokens, long long experts) {
   const long long out = features * (mode == EXPERT_WGRAD ? rows * experts : tokens);  // output elements
   if (f32) return features > 128 && out >= (mode == EXPERT_WGRAD ? 4500000 : 1250000);
@@ -878,11 +884,13 @@ bool expert_pair(ExpertMode mode, bool f32, long long features, long long rows, 
 // Whether fp32 operands are split by the product kernel itself or packed into planes before it.  Packing
 // reads 4 and writes 6 bytes of each weight before 6 are loaded, for every tile that loads them; the
 // kernel's own split reads 4, but anew for each tile, whose rows are at most 64.  Measured (us, packed ->
-// split), products with 16 experts of 1536 x 768: 8 tokens an expert 69.5 -> 43.2, 64 tokens 74.1 -> 48.8, 128
-// tokens 79.4 -> 85.8; input gradients 69.1 -> 43.6, 73.8 -> 49.4, 78.8 -> 87.6; 64 experts, 24 tokens in all
-// 94.2 -> 42.0.  Gradients pack only tokens, and have more tiles the narrower they are: they split where the
-// packing launch is what costs (48 experts of 200 x 328, 201 tokens 18.3 -> 14.3; 16 of 1536 x 768, 8 tokens
-// an expert 45.0 -> 68.3).
+// split), products with 16 experts of 1536 x 768: 8 tokens an expert 69.5 -> 43.2, 64 tokens 73.2 -> 47.2, 80
+// tokens 74.8 -> 63.7, 128 tokens 78.8 -> 68.4 (79.4 -> 85.8 where the router is uneven); input gradients 64 tokens
+// 71.9 -> 47.7, 80 tokens 88.6 -> 80.7, 128 tokens 80.8 -> 87.8; 64 experts, 24 tokens in all 94.2 -> 42.0.
+// Gradients pack only tokens, and have more tiles the narrower they are: they split where the packing
+// launch is what costs (16 experts, 8 tokens each, millions of elements 3.1: 18.7 -> 16.3, 3.9: 21.4 -> 19.1, 4.1:
+// 22.1 -> 20.5, 4.7: 19.4 -> 20.5, 5.5: 21.8 -> 24.5, 9.4: 25.7 -> 37.0; 48 tokens each 3.9: 21.3 -> 20.1, 4.7:
+// 19.1 -> 21.6).
 bool expert_split(ExpertMode mode, long long outputs, long long tokens, long long experts) {
   return tokens <= 64 * experts && (mode != EXPERT_WGRAD || outputs <= 4000000);
 }
