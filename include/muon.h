@@ -34,7 +34,8 @@
  *     (non-finite norm, a kernel wait that ran out) are reported by
  *     muon_get_status() after the stream has been synchronised.
  *   - Two calls on the same context must not run concurrently on different
- *     streams: they share the workspace.  A context is used from one host
+ *     streams: they share the workspace.  Replays of graphs that captured
+ *     its calls count as calls.  A context is used from one host
  *     thread at a time; separate contexts are independent.
  *   - Work a call puts on the context's internal streams (the uploads of
  *     muon_step_groups_host) starts after what is already queued on `stream`

@@ -44,7 +44,11 @@ def expert_linear(x, w, offsets, muon, grad_into=None):
 
     x: [tokens, cols], rows sorted by expert; w: [experts, rows, cols]; offsets: int32 CUDA
     [experts + 1] (rows offsets[e] .. offsets[e+1]-1 belong to expert e; rows of no expert give and
-    receive zeros, and so does everything if the offsets are bad, which muon.status() reports); muon: the libmuon context whose scratch the products use.  bf16 or fp32.
+    receive zeros, and so does everything if the offsets are bad, which muon.status() reports); muon:
+    the libmuon context whose scratch the products use.  bf16 or fp32.
+    fp32 operands, and bf16 ones whose rows do not start on 16-byte boundaries, may be repacked into that scratch
+    (up to 6 bytes an element of x and w, held until the context is closed), so layers that run at the same time on
+    different streams, backward passes and replayed graphs included, need a context each.
     grad_into: an fp32 [experts, rows, cols] buffer that the weight gradient is added to, over as many
     backward passes as one likes, if w requires a gradient.  w.grad then stays None, so an optimizer that
     reads it passes w over: hand the buffer to ``MuonAdamW.step`` as w's gradient, or name it in
