@@ -531,7 +531,8 @@ class Muon:
 
         W, G, M: lists of same-shape 2-D tensors (or 3-D stacks) as in ``step``; rows contiguous, any
         row stride, so views of larger weights may be stepped.  The shorter side of a block is at
-        most 128, the longer one at most 5632 (bf16) or 2560 (fp32), or more (``check_block``).  Up to MAX_BATCH matrices a call, none of which may overlap another.
+        most 128, the longer one at most 5632 (bf16) or 2560 (fp32), or more (``check_block``).  Up to
+        MAX_BATCH matrices a call, none of which may overlap another.
         """
         b = self._blocks(W, G, M, block)
         h = self.hparams(**hp)

@@ -96,6 +96,9 @@ class MuonAdamW:
         A parameter whose name is missing from ``grads`` or maps to None (frozen, or unused
         in this backward pass) is left untouched: its weights get no decay, its Muon momentum
         no step and its AdamW moments and step count stay as they are.
+
+        ``ctx.status()`` afterwards covers every block of the step, and the whole matrices of its last call
+        (of up to MAX_GROUPS groups).
         """
         self.t += 1
         groups = []
@@ -157,8 +160,8 @@ def torch_optimizer(named_params, mode="both", inner=None, main_grads=None, **kw
     ``.grad`` is None at ``step()`` are skipped, as ``torch.optim.AdamW`` skips them: no decay,
     no momentum step, no moment update.  ``main_grads`` ({name: buffer}) names the parameters whose
     gradients are accumulated elsewhere (``expert_linear(..., grad_into=buffer)``, which leaves ``.grad``
-    None): ``step()`` reads their buffers and ``zero_grad()`` clears them.  ``inner`` replaces the MuonAdamW instance (host-side
-    tests only).
+    None): ``step()`` reads their buffers and ``zero_grad()`` clears them.  ``inner`` replaces the
+    MuonAdamW instance (host-side tests only).
     """
     import torch
 
