@@ -246,8 +246,11 @@ __device__ __forceinline__ void store_rows(const ExpertParams& P, long long at, 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (16 * h >= nv) break;
-    // the map ends where the output does; a box may only be cut short there
-    if (P.vec && (P.beta == 0.f || P.beta == 1.f) && (16 * h + 16 <= nv || rows_end)) {
+    // The map ends where the output does; a box may only be cut short there.  A store cuts the columns at a
+    // 16-byte boundary, behind which up to three elements of the caller's may begin: then the last columns go
+    // out one by one.
+    if (P.vec && (P.beta == 0.f || P.beta == 1.f) && (16 * h + 16 <= nv || rows_end) &&
+        (nf >= 32 || P.features % 4 == 0)) {
       const uint32_t buf = stage + (boxes++ & 1) * 2048u;
       if (lane == 0) bulk_wait_group_read<1>();  // the box before the last one has left this buffer
       __syncwarp();
